@@ -199,16 +199,12 @@ def _dequantized(held, scales, row, fmt, dtype):
     return v if row is None else v * row.to(dtype)[..., None]
 
 
-def _pair_table():
-    """byte -> the 8-bit floats of its two e2m1 codes, in one 16-bit word."""
-    v = torch.tensor(_E2M1, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8).short()
-    return (v[None, :] | (v[:, None] << 8)).flatten()
-
-
-def _held_values(held, fmt, pairs):
+def _held_values(held, fmt):
     """What the held codes stand for, as 8-bit floats."""
     if fmt == "mxfp8":
         return held.view(torch.float8_e4m3fn)
+    v = torch.tensor(_E2M1, device=held.device).to(torch.float8_e4m3fn).view(torch.uint8).short()
+    pairs = (v[None, :] | (v[:, None] << 8)).flatten()  # byte -> the two values' bytes
     return pairs.index_select(0, held.flatten().int()).view(torch.float8_e4m3fn).reshape(*held.shape[:-1], -1)
 
 
@@ -262,7 +258,6 @@ def prepare(case, seed):
         return s
     dt = _dtype(case)
     rows = case["rows"]
-    s["pairs"] = _pair_table()  # looked up in run(): made there it would wait for its copy from the host
     if case["op"] in ("swiglu", "swiglu_bwd"):
         s["x"] = (_randn(g, rows, 2 * case["F"]) * 1.5).to(dt)
         if case["op"] == "swiglu_bwd":
@@ -383,7 +378,7 @@ def _run_own(s, op):
         codes, scales, row, h, rstd, post_rstd = bsq.bsq_norm_quantize(
             s["x"], fmts[c["fmt"]], s["weight"], residual=s["residual"], gate=s["gate"], post_weight=s["post_weight"],
             residual_scale=c["scale"], eps=EPS)
-        out = {"codes": _held_values(codes, c["fmt"], s["pairs"]), "scales": _scales(scales, c["fmt"]), "rstd": rstd}
+        out = {"codes": _held_values(codes, c["fmt"]), "scales": _scales(scales, c["fmt"]), "rstd": rstd}
         return _norm_out(s, out, row, h, post_rstd)
     if op == "norm_bwd":
         got = bsq.bsq_norm_quantize_backward(
@@ -395,7 +390,7 @@ def _run_own(s, op):
         return {k: v for k, v in out.items() if v is not None}
     if op == "swiglu":
         codes, scales, row = bsq.bsq_swiglu_quantize(s["x"], fmts[c["fmt"]])
-        out = {"codes": _held_values(codes, c["fmt"], s["pairs"]), "scales": _scales(scales, c["fmt"])}
+        out = {"codes": _held_values(codes, c["fmt"]), "scales": _scales(scales, c["fmt"])}
         return out if row is None else {**out, "row_scale": row}
     return {"grad_x": bsq.bsq_swiglu_backward(s["grad_y"], s["x"])}
 
