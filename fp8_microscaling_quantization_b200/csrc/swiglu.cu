@@ -17,22 +17,46 @@
 
 namespace bsq {
 
-// s = 1 / (1 + 2**(-g log2(e))) by the hardware's base-2 exponential and
-// reciprocal, 2 and 1 last places off; the rounded exponent adds |g| * 2**-23
-// of the power: below g = -88 the power overflows to
-// infinity and its reciprocal is 0; above 87 it flushes to 0 and s is 1.
-__device__ __forceinline__ float sigmoid(float g) {
-    float p, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(g * -1.44269504f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + p));
-    return s;
-}
+// s = 1 / (1 + exp(-g)), of the backward pass: HBM bounds that either way
+// (16384 x 2048 bf16 55.5 us, with the hardware's approximations 56).
+__device__ __forceinline__ float sigmoid(float g) { return __frcp_rn(1.0f + expf(-g)); }
 
-// silu(g) * u of 8 elements, into g.
-__device__ __forceinline__ void swiglu8(float g[8], const float u[8]) {
+// silu(g) * u of 8 elements, into g.  The division is the hardware's reciprocal
+// (1 last place off); where 1 + exp(-g) passes 2**126, at g < -87.3, it gives 0.
+//
+// bf16: a rounded product g * log2(e) would put |g| * 2**-23 of error into the
+// power, so it is split.  With H = log2(e) to 16 bits, t = -g * H is exact (8
+// bits times 16) and p = 2**t is the hardware's (2 last places off); the rest
+// of log2(e) makes the power p exp(-q), q = g * c, and with |q| < 5e-4 that is
+// p (1 - q), give or take q**2 / 2.  (16384 x 2048 bf16 to MXFP8 31.4 us, to
+// NVFP4 36.9, with the rounded product 31.1 and 37.0; with expf 41 and 45.)
+__device__ __forceinline__ void swiglu8(float g[8], const float u[8], const uint16_t*) {
+    constexpr float kH = 1.44268798828125f;  // 47274 / 2**15
+    constexpr float kC = 4.8884951e-06f;     // (log2(e) - kH) ln(2)
+    const float2 h = make_float2(-kH, -kH), c = make_float2(-kC, -kC), one = make_float2(1.0f, 1.0f);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 v = make_float2(g[j], g[j + 1]), t = mul_f32x2(v, h);
+        float2 p, s;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(t.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(t.y));
+        p = fma_f32x2(p, fma_f32x2(v, c, one), one);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(p.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(p.y));
+        const float2 y = mul_f32x2(v, s);
+        g[j] = y.x;
+        g[j + 1] = y.y;
+    }
+    mul8(g, u);
+}
+// fp32: HBM hides expf (16384 x 2048 to MXFP8 51.8 us, without it 51.5).
+__device__ __forceinline__ void swiglu8(float g[8], const float u[8], const float*) {
     float s[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = sigmoid(g[j]);
+    for (int j = 0; j < 8; ++j) {
+        const float x = 1.0f + expf(-g[j]);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[j]) : "f"(x));
+    }
     mul8(g, s);
     mul8(g, u);
 }
@@ -63,7 +87,7 @@ __global__ void __launch_bounds__(MAXT) swiglu_quant_kernel(const T* __restrict_
             float g[8], u[8];
             rg[i].get(g);
             ru[i].get(u);
-            swiglu8(g, u);
+            swiglu8(g, u, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[i][j] = g[j];
         }
@@ -75,9 +99,8 @@ __global__ void __launch_bounds__(MAXT) swiglu_quant_kernel(const T* __restrict_
 
 // The formats without a row scale: chunks of all rows in one stream.  One
 // chunk per thread at a time, at full occupancy: the loads of other warps
-// cover a warp's arithmetic (16384 x 2048 bf16 to MXFP8 31.5 us, 82% of the
-// HBM copy rate; two or four chunks in flight per thread 35 us, fp32 24 and
-// 30 to 37 us).
+// cover a warp's arithmetic (16384 x 2048 bf16 to MXFP8 31.4 us, 82% of the
+// HBM copy rate; two or four chunks in flight per thread 35 us).
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads, 8) swiglu_flat_kernel(const T* __restrict__ x, FastDiv row_chunks, int64_t nchunks,
                                                                   int F, uint8_t* __restrict__ codes,
@@ -97,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 8) swiglu_flat_kernel(const T* __res
         float g[8], u[8];
         rg.get(g);
         ru.get(u);
-        swiglu8(g, u);
+        swiglu8(g, u, x);
         uint32_t s;
         const uint2 w = chunk_codes<FMT>(g, group_max<4>(amax8(g)), 0.0f, 0.0f, &s);
         if (base + lane < nchunks) {

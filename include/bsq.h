@@ -371,7 +371,8 @@ bsq_status bsq_norm_quantize_backward(const void* grad_y, const void* grad_h, co
 /* ------------------------------------------------- gated activation -------
  * x [rows, 2F] holds the gate half g (columns [0, F)) and the up half u
  * ([F, 2F)) of a fused gate/up product (bf16 or fp32, 16-byte aligned):
- *   y = silu(g) * u = g / (1 + exp(-g)) * u      in binary32,
+ *   y = silu(g) * u = g / (1 + exp(-g)) * u      in binary32
+ * (13 * 2**-24 of y off at most; 0 where g < -87.3, past the reciprocal's range),
  * quantized by the rules of bsq_quantize_<fmt> for a binary32 input, fmt
  * BSQ_NVFP4 (F % 16 == 0), BSQ_MXFP4 or BSQ_MXFP8 (F % 32 == 0), F <= 32768.
  * codes, scales and row_scale as there.  (The quantization pages take the
