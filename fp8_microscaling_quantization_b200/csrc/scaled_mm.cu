@@ -58,8 +58,10 @@
 //     over distributed shared memory, in rank order.
 //
 // Every mbarrier wait is bounded (about a second): the thread records
-// BSQ_DEVERR_TIMEOUT in the error word and raises a CTA-wide abort flag, all
-// roles wind down, outstanding loads and MMAs are drained (again bounded) and
+// BSQ_DEVERR_TIMEOUT in the error word and raises a CTA-wide abort flag, and all
+// roles leave their loops.  The MMA warp waits for its MMAs; when the roles of
+// all CTAs of a pair have stopped, the loads in flight are waited for too, by
+// what each role had done (pipeline_drain.h; one limit for all of them), and
 // tensor memory is freed before the CTA exits.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -72,6 +74,7 @@
 #include "debug.cuh"
 #include "common.cuh"
 #include "host_util.h"
+#include "pipeline_drain.h"
 #include "scaled_tc.cuh"
 
 namespace bsq {
@@ -135,7 +138,7 @@ struct Plan {
     static constexpr int kSlots = (CG == 2) ? 2 : STAGES;
     static constexpr int kSlotCols = 16 + 16 * XBLK;
     static_assert(kScaleCols + kSlots * kSlotCols <= (int)kTmemCols && kAccStep + TN <= kScaleCols, "tensor memory plan");
-    static_assert(kNumBars * 8 + 16 <= 1024 && kOutOff % 1024 == 0 && STAGES >= 3, "shared memory plan");
+    static_assert(kNumBars * 8 + 64 <= 1024 && kOutOff % 1024 == 0 && STAGES >= 3, "shared memory plan");
 };
 
 struct Args {
@@ -173,6 +176,11 @@ struct Shared {
     uint64_t* drain;
     uint32_t* tmem_slot;
     volatile int* abort;
+    // what each CTA of a pair (a single CTA: [0]) had done when its roles had stopped
+    int* issued;      // [2] k-steps whose codes it has loaded
+    int* fenced;      // [2] k-steps whose scales it has handed over
+    int* gave_up;     // [2]
+    int* raw_issued;  // chunks of scale rows that this CTA has loaded
     int* tt_prefix;  // [E + 1] first token tile of each expert
     int* seg;        // [E + 1] seg[e] = first row of expert e, seg[E] = offs[E-1]
     float* row;      // [kEpiWarps][kRowFloats] row scales of the tokens that each epilogue warp drains
@@ -197,6 +205,10 @@ __device__ __forceinline__ Shared carve(uint8_t* raw) {
     s.drain = s.acc_full + 2;
     s.tmem_slot = reinterpret_cast<uint32_t*>(bars + P::kNumBars);
     s.abort = reinterpret_cast<volatile int*>(s.tmem_slot + 1);
+    s.issued = reinterpret_cast<int*>(s.tmem_slot + 4);
+    s.fenced = s.issued + 2;
+    s.gave_up = s.issued + 4;
+    s.raw_issued = s.issued + 6;
     s.row = reinterpret_cast<float*>(base + P::kBarOff + 1024);
     s.tt_prefix = reinterpret_cast<int*>(s.row + kEpiWarps * P::kRowFloats);
     s.seg = s.tt_prefix + kMaxExperts + 1;
@@ -570,6 +582,32 @@ __device__ __forceinline__ void drain_tokens(const CUtensorMap* tmap_out, const 
     }
 }
 
+// Waits, by one thread of each CTA and for a second at most, for the loads that
+// are in flight when the roles of all CTAs have stopped: the codes of both CTAs
+// of a pair, which count on the leader's barriers, and the CTA's own scale rows.
+template <int KIND, int CG, bool RAW>
+__device__ __forceinline__ void drain_loads(const Shared& sh, uint32_t bytes, int rank) {
+    constexpr int S = Plan<KIND, CG, RAW>::STAGES;
+    const uint64_t t0 = globaltimer_ns();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const uint64_t spent = globaltimer_ns() - t0;
+        mbar_wait(bar, parity, spent < kWaitNs ? kWaitNs - spent : 0);
+    };
+    if (rank == 0) {
+        const int first = drain_first(sh.issued, CG, S), last = drain_last(sh.issued, CG);
+        for (int j = first; j < last; ++j) {
+            const PhaseDebt d = phase_debt(j, sh.issued, CG, bytes, sh.fenced, CG);
+            uint64_t* bar = &sh.full[j % S];
+            if (d.expect) mbar_arrive_expect_tx(bar, d.expect);
+            if (d.complete) mbar_complete_tx(bar, d.complete);
+            if (d.arrivals) mbar_arrive_n(bar, d.arrivals);
+        }
+        for (int j = first; j < last; ++j) wait(&sh.full[j % S], (uint32_t)(j / S) & 1);
+    }
+    if (RAW)  // the thread that loads scale rows names their bytes: nothing else is owed
+        for (int j = max(0, *sh.raw_issued - 2); j < *sh.raw_issued; ++j) wait(&sh.raw[j & 1], (uint32_t)(j >> 1) & 1);
+}
+
 __device__ __forceinline__ float lds_cluster_f32(uint32_t cluster_addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
@@ -728,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ codes of both operands
         // one box of weights and one of tokens per k-step; converged, as the
         // MMA warp below
-        int64_t it = 0, rit = 0;
+        int it = 0, rit = 0;
         int s = 0, rs = 0;
         uint32_t ph = 1, rph = 1;
         bool ok = true;
@@ -777,26 +815,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (!ok && leader && lane == 0) {
-            // drain the loads still in flight (a pair's loads all count on the
-            // leader's barriers); a stage whose scales were given up never
-            // completes, and its wait ends at the time limit, long after its
-            // bytes have landed
-            for (int64_t j = (it > P::STAGES ? it - P::STAGES : 0); j < it; ++j)
-                mbar_wait(&sh.full[j % P::STAGES], (uint32_t)((j / P::STAGES) & 1), kWaitNs);
+        if (lane == 0) {
+            sh.issued[rank] = it;
+            *sh.raw_issued = rit;
         }
-        if (RAW && !ok && lane == 0)
-            for (int64_t j = (rit > 2 ? rit - 2 : 0); j < rit; ++j)
-                mbar_wait(&sh.raw[j & 1], (uint32_t)((j >> 1) & 1), kWaitNs);
     } else if (warp == kFenceWarp) {
         // ----------------------------- scales: generic stores -> tensor core
         if (lane == 0) {
             int my_tiles = 0;
             if (wk.num > wk.t0) my_tiles = (wk.num - 1 - wk.t0) / wk.step + 1;
-            const int64_t items = (int64_t)my_tiles * (wk.k1 - wk.k0);
-            int s = 0;
+            const int items = my_tiles * (wk.k1 - wk.k0);
+            int s = 0, it = 0;
             uint32_t ph = 0;
-            for (int64_t it = 0; it < items; ++it) {
+            for (; it < items; ++it) {
                 if (!wait_bar(&sh.scales[s], ph, sh, args)) break;
                 fence_proxy_async_smem();
                 arrive_leader<CG>(&sh.full[s]);
@@ -805,6 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ph ^= 1;
                 }
             }
+            sh.fenced[rank] = it;
         }
     } else if (leader) {
         // ------------------------------------------------ MMA (leader only)
@@ -889,6 +921,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) {
+        if (threadIdx.x == 0) {  // to the peer: what this CTA has done
+            const uint32_t to = mapa_shared(smem_u32(sh.issued + rank), rank ^ 1);
+            sh.gave_up[rank] = *sh.abort;
+            st_cluster(to, sh.issued[rank]);
+            st_cluster(to + 8, sh.fenced[rank]);
+            st_cluster(to + 16, *sh.abort);
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while its peer may still touch it
+    }
+    if (CG == 2 ? (sh.gave_up[0] | sh.gave_up[1]) != 0 : *sh.abort != 0) {
+        if (threadIdx.x == 0) drain_loads<KIND, CG, RAW>(sh, args.w_tx + P::kX, rank);
+        __syncwarp();
+        if (CG == 2) cluster_sync();  // the leader has waited for its peer's loads
+        else __syncthreads();
+    }
     if (CG == 1 && split > 1) {
         // add the cluster's partial sums in rank order, each CTA for its share
         // of the features
@@ -911,7 +960,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         cluster_sync();  // no CTA leaves while a peer may still read it
     }
-    if (CG == 2) cluster_sync();  // no CTA leaves while its peer may still touch it
     tc_fence_after();
     if (warp == kMmaWarp) {
         if (CG == 1) tmem_dealloc(tmem, kTmemCols);
