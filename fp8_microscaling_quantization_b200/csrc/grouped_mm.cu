@@ -42,9 +42,11 @@
 // lies on the contraction there and is folded into the dequantized weight.
 //
 // Every mbarrier wait gives up after about a second: the thread records
-// BSQ_DEVERR_TIMEOUT in the error word and raises a CTA-wide abort flag, all
-// roles wind down, outstanding TMA loads and MMAs are drained (again with a
-// time limit) and tensor memory is freed before the CTA exits.
+// BSQ_DEVERR_TIMEOUT in the error word and raises a CTA-wide abort flag, and all
+// roles leave their loops.  The MMA thread waits for its MMAs; when the roles of
+// all CTAs of a pair have stopped, the loads in flight are waited for too, by
+// what each role had done (pipeline_drain.h; one limit for all of them), and
+// tensor memory is freed before the CTA exits.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -56,6 +58,7 @@
 #include "debug.cuh"
 #include "formats.cuh"
 #include "host_util.h"
+#include "pipeline_drain.h"
 #include "tcgen05.cuh"
 
 namespace bsq {
@@ -112,7 +115,7 @@ struct Plan {
     static constexpr size_t kBarOffset = (size_t)STAGES * kStage;
     static constexpr int kNumBars = 2 * STAGES + 5;
     static constexpr size_t kSmemBytes = 1024 /* alignment slack */ + kBarOffset + kNumBars * 8 +
-                                         16 /* tmem slot, flags */ + 4 * (2 * kMaxExperts + 2);
+                                         16 /* tmem slot, flags */ + 4 * (4 + 2 * kDqWarps) + 4 * (2 * kMaxExperts + 2);
 };
 
 struct Args {
@@ -142,6 +145,10 @@ struct Shared {
     uint64_t* drain;
     uint32_t* tmem_slot;
     volatile int* abort;
+    // what each CTA of a pair (a single CTA: [0]) had done when its roles had stopped
+    int* issued;   // [2] k-steps whose activations it has loaded
+    int* gave_up;  // [2]
+    int* stored;   // [2][kDqWarps] k-steps that each producer warp has stored
     int* tt_prefix;  // [E + 1] first token tile of each expert
     int* seg;        // [E + 1] seg[e] = first row of expert e, seg[E] = offs[E-1]
 };
@@ -160,7 +167,10 @@ __device__ __forceinline__ Shared carve(uint8_t* raw) {
     s.drain = s.acc_empty + 2;
     s.tmem_slot = reinterpret_cast<uint32_t*>(bars + P::kNumBars);
     s.abort = reinterpret_cast<volatile int*>(s.tmem_slot + 1);
-    s.tt_prefix = reinterpret_cast<int*>(s.tmem_slot + 4);
+    s.issued = reinterpret_cast<int*>(s.tmem_slot + 4);
+    s.gave_up = s.issued + 2;
+    s.stored = s.issued + 4;
+    s.tt_prefix = s.stored + 2 * kDqWarps;
     s.seg = s.tt_prefix + kMaxExperts + 1;
     return s;
 }
@@ -369,6 +379,44 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
     else mbar_arrive_cluster(mapa_shared(smem_u32(bar), 0));
 }
 
+// A CTA's activation rows of a tile's first and second MMA (the tokens rounded
+// up to 16, its share of them) and the boxes of XBOX rows that hold them.
+struct XRows {
+    int h0, h1, nbox0, nbox1;
+};
+template <int CG>
+__device__ __forceinline__ XRows x_rows(int ntok) {
+    XRows x;
+    x.h0 = ((min(ntok, TN) + 15) & ~15) / CG;
+    x.h1 = (CG == 2 && ntok > TN) ? ((ntok - TN + 15) & ~15) / CG : 0;
+    x.nbox0 = (x.h0 + XBOX - 1) / XBOX;
+    x.nbox1 = (x.h1 + XBOX - 1) / XBOX;
+    return x;
+}
+
+// Waits, by the leader and for a second at most, for the loads that are in
+// flight when the roles of all CTAs have stopped (a pair's count on the
+// leader's barriers).
+template <int CG>
+__device__ __forceinline__ void drain_loads(const Shared& sh, int group, int ngroups, int f_tiles, int k_steps, int E) {
+    constexpr int S = Plan<CG>::STAGES;
+    const uint64_t t0 = globaltimer_ns();
+    const int first = drain_first(sh.issued, CG, S), last = drain_last(sh.issued, CG);
+    for (int j = first; j < last; ++j) {
+        const XRows x = x_rows<CG>(decode_tile<CG>(group + j / k_steps * ngroups, f_tiles, E, sh).ntok);
+        const PhaseDebt d =
+            phase_debt(j, sh.issued, CG, (uint32_t)(x.nbox0 + x.nbox1) * kXBoxBytes, sh.stored, CG * kDqWarps);
+        uint64_t* bar = &sh.full[j % S];
+        if (d.expect) mbar_arrive_expect_tx(bar, d.expect);
+        if (d.complete) mbar_complete_tx(bar, d.complete);
+        if (d.arrivals) mbar_arrive_n(bar, d.arrivals);
+    }
+    for (int j = first; j < last; ++j) {
+        const uint64_t spent = globaltimer_ns() - t0;
+        mbar_wait(&sh.full[j % S], (uint32_t)(j / S) & 1, spent < kWaitNs ? kWaitNs - spent : 0);
+    }
+}
+
 template <int FMT, int DIR, int CG>
 __global__ void __launch_bounds__(kThreads, 1) grouped_mm_kernel(const __grid_constant__ CUtensorMap tmap_x, Args args) {
     using P = Plan<CG>;
@@ -526,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_mm_kernel(const __grid_co
                     const int s = i % P::STAGES;
                     if (!wait_bar_warp(&sh.empty[s], ((i / P::STAGES) & 1) ^ 1, sh, args)) {
                         ok = false;
+                        if (lane == 0) sh.stored[(int)rank * kDqWarps + warp - kEpiWarps] = i;
                     } else {
                         store_unit<DIR>(v, st_base + s * P::kStage, dq);
                         fence_proxy_async_smem();
@@ -535,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_mm_kernel(const __grid_co
                 }
             }
         }
+        if (ok && lane == 0) sh.stored[(int)rank * kDqWarps + warp - kEpiWarps] = items;
     } else if (warp == kTmaWarp) {
         // ------------------------------------------- B (activation) producer
         if (lane == 0) {
@@ -542,12 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_mm_kernel(const __grid_co
             bool ok = true;
             for (int t = group; t < num_tiles && ok; t += ngroups) {
                 const Tile ti = decode_tile<CG>(t, f_tiles, E, sh);
-                // tokens of the tile's first and second MMA, rounded up to 16,
-                // and this CTA's share (rows) of each
-                const int n0 = (min(ti.ntok, TN) + 15) & ~15;
-                const int n1 = (CG == 2 && ti.ntok > TN) ? ((ti.ntok - TN + 15) & ~15) : 0;
-                const int h0 = n0 / CG, h1 = n1 / CG;
-                const int nbox0 = (h0 + XBOX - 1) / XBOX, nbox1 = (h1 + XBOX - 1) / XBOX;
+                const XRows x = x_rows<CG>(ti.ntok);
                 for (int ks = 0; ks < k_steps; ++ks, ++it) {
                     const int s = it % P::STAGES;
                     if (!wait_bar(&sh.empty[s], ((it / P::STAGES) & 1) ^ 1, sh, args)) {
@@ -556,32 +601,25 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_mm_kernel(const __grid_co
                     }
                     uint8_t* dst = sh.stage + s * P::kStage + kWStage;
                     if (CG == 1) {
-                        const int nbox = nbox0;
+                        const int nbox = x.nbox0;
                         mbar_arrive_expect_tx(&sh.full[s], nbox * kXBoxBytes);
                         for (int b = 0; b < nbox; ++b)
                             tma_load_2d(dst + b * kXBoxBytes, &tmap_x, &sh.full[s], ks * BK, ti.tok0 + b * XBOX);
                     } else {
                         // both CTAs' boxes complete on the leader's barrier; the
                         // second MMA's rows go kXHalf into the slot
-                        if (leader) mbar_arrive_expect_tx(&sh.full[s], 2 * (nbox0 + nbox1) * kXBoxBytes);
+                        if (leader) mbar_arrive_expect_tx(&sh.full[s], 2 * (x.nbox0 + x.nbox1) * kXBoxBytes);
                         const uint32_t bar = mapa_shared(smem_u32(&sh.full[s]), 0);
-                        for (int b = 0; b < nbox0; ++b)
+                        for (int b = 0; b < x.nbox0; ++b)
                             tma_load_2d_pair(dst + b * kXBoxBytes, &tmap_x, bar, ks * BK,
-                                             ti.tok0 + (int)rank * h0 + b * XBOX);
-                        for (int b = 0; b < nbox1; ++b)
+                                             ti.tok0 + (int)rank * x.h0 + b * XBOX);
+                        for (int b = 0; b < x.nbox1; ++b)
                             tma_load_2d_pair(dst + P::kXHalf + b * kXBoxBytes, &tmap_x, bar, ks * BK,
-                                             ti.tok0 + TN + (int)rank * h1 + b * XBOX);
+                                             ti.tok0 + TN + (int)rank * x.h1 + b * XBOX);
                     }
                 }
             }
-            if (!ok && leader) {
-                // drain the loads still in flight (a pair's loads all count on
-                // the leader's barriers); a stage whose producer warps gave up
-                // never completes, and its wait ends at the time limit, long
-                // after its bytes have landed
-                for (int j = (it > P::STAGES ? it - P::STAGES : 0); j < it; ++j)
-                    mbar_wait(&sh.full[j % P::STAGES], (j / P::STAGES) & 1, kWaitNs);
-            }
+            sh.issued[rank] = it;
         }
     } else {
         // ------------------------------------------------ MMA (leader only)
@@ -677,7 +715,40 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_mm_kernel(const __grid_co
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync();  // no CTA leaves while its peer may still touch it
+    {
+        // from the launch's values again, unseen by the compiler: kept across
+        // the roles' loops they would spill there
+        uintptr_t smem = reinterpret_cast<uintptr_t>(smem_raw);
+        uint32_t cta, ctas;
+        int width = args.N, depth = args.K;
+        asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta));
+        asm volatile("mov.u32 %0, %%nctaid.x;" : "=r"(ctas));
+        asm volatile("" : "+l"(smem), "+r"(width), "+r"(depth));
+        const Shared end = carve<CG>(reinterpret_cast<uint8_t*>(smem));
+        const int me = CG == 2 ? (int)cluster_ctarank() : 0;
+        if (CG == 2) {
+            if (threadIdx.x < 32) {  // to the peer: what this CTA has done
+                const uint32_t to = mapa_shared(smem_u32(end.issued), me ^ 1);
+                for (int i = threadIdx.x; i < kDqWarps; i += 32)
+                    st_cluster(to + (4 + me * kDqWarps + i) * 4, end.stored[me * kDqWarps + i]);
+                if (threadIdx.x == 0) {
+                    end.gave_up[me] = *end.abort;
+                    st_cluster(to + me * 4, end.issued[me]);
+                    st_cluster(to + (2 + me) * 4, *end.abort);
+                }
+                __syncwarp();
+            }
+            cluster_sync();  // no CTA leaves while its peer may still touch it
+        }
+        if (CG == 2 ? (end.gave_up[0] | end.gave_up[1]) != 0 : *end.abort != 0) {
+            if (threadIdx.x == 0 && me == 0) {
+                const int out = (DIR == BSQ_FWD) ? width : depth, contr = (DIR == BSQ_FWD) ? depth : width;
+                drain_loads<CG>(end, (int)cta / CG, (int)ctas / CG, out / (WM * CG), contr / BK, args.E);
+            }
+            __syncwarp();
+            if (CG == 2) cluster_sync();  // the leader has waited for its peer's loads
+        }
+    }
     tc_fence_after();
     if (warp == kMmaWarp) {
         if (CG == 1) tmem_dealloc(tmem, kTmemCols);

@@ -43,7 +43,7 @@ def test_a_drain_that_goes_by_the_load_role_alone_leaves_loads_in_flight(model, 
     assert gave_up > 2000 and left > 0
 
 
-@pytest.mark.parametrize("name", ["scaled_mm.cu"])
+@pytest.mark.parametrize("name", ["scaled_mm.cu", "grouped_mm.cu"])
 def test_the_products_drain_by_the_counts(name):
     """A kernel decides on the drain when its roles have joined (the CTA's last
     barrier but one), by the arithmetic that the model checks."""
