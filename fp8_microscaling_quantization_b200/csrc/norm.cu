@@ -47,7 +47,6 @@ struct NormArgs {
     const T* gate;      // NULL: 1
     int64_t rows;
     int C;
-    float inv_c;  // 1 / C
     float scale, eps;
     const float* post_weight;  // NULL: no norm after the block
     const float* weight;
@@ -93,6 +92,13 @@ struct Chunks {
     }
 };
 
+// (sum / C + eps)^-1/2, each step rounded to nearest: a row's factor is in all
+// of its codes, so it is multiplied in by itself too, not folded into the
+// residual scale or the weights first.
+__device__ __forceinline__ float rms_factor(float sum, int C, float eps) {
+    return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)C), eps));
+}
+
 // KEEP: a thread's elements of the inputs stay in registers, all loads issued
 // first; else (rows too long for that) they are read where they are used,
 // again from L2 the second time.
@@ -127,9 +133,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_quant_kernel(NormArgs<T> p) {
                 rx[i].get(v);
                 ss = ch.valid(i) ? dot8(v, v, ss) : ss;
             }
-            post = rsqrtf(red.sum(ss.x + ss.y) * p.inv_c + p.eps);
+            post = rms_factor(red.sum(ss.x + ss.y), p.C, p.eps);
         }
-        const float scale = p.scale * post;
         float h[NCH][8];
         float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -144,6 +149,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_quant_kernel(NormArgs<T> p) {
             if (post_norm) {
                 float w[8];
                 load_weight(p.post_weight, at, w);
+                mul8(h[i], post);
                 mul8(h[i], w);
             }
             if (gated) {
@@ -154,20 +160,20 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_quant_kernel(NormArgs<T> p) {
             if (summed) {
                 float r[8];
                 rr[i].get(r);
-                fma8(h[i], h[i], scale, r);
+                fma8(h[i], h[i], p.scale, r);
             } else {
-                mul8(h[i], scale);
+                mul8(h[i], p.scale);
             }
             ss = ch.valid(i) ? dot8(h[i], h[i], ss) : ss;
             if (p.h && ch.stored(i, row, p.rows)) store8(p.h + base + at, h[i]);
         }
-        const float rstd = rsqrtf(red.sum(ss.x + ss.y) * p.inv_c + p.eps);
+        const float rstd = rms_factor(red.sum(ss.x + ss.y), p.C, p.eps);
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const uint32_t at = ch.at(i);
             float w[8];
             load_weight(p.weight, at, w);
-            mul8(w, rstd);
+            mul8(h[i], rstd);
             mul8(h[i], w);
         }
         const float g = quantize_row<FMT, NCH>(h, p.C / 8, p.codes + base * kCodeBits / 8, p.scales + base / kBlock, red);
@@ -224,7 +230,6 @@ struct NormBwdArgs {
     float scale;
     int64_t rows;
     int C;
-    float inv_c;  // 1 / C
     T* grad_residual;  // NULL: not stored
     T* grad_x;         // NULL: not stored
     T* grad_gate;
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormBwdArgs<T> p, bool s
             mul8(d[i], w);
             dot = ch.valid(i) ? dot8(d[i], hh, dot) : dot;
         }
-        const float mean = red.sum(dot.x + dot.y) * p.inv_c;
+        const float mean = __fdiv_rn(red.sum(dot.x + dot.y), (float)p.C);
         const float hm = -(rstd * mean) * rstd;  // dh = gh + rstd * a - (rstd^2 mean) h
         const int64_t next = min(row + gridDim.x, p.rows - 1);
         dot = make_float2(0.0f, 0.0f);
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormBwdArgs<T> p, bool s
             }
         }
         if (post_norm) {
-            const float m = red.sum(dot.x + dot.y) * p.inv_c;
+            const float m = __fdiv_rn(red.sum(dot.x + dot.y), (float)p.C);
             const float xm = -(post * m) * post;  // grad_x = post * b - (post^2 mean) x
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
@@ -526,7 +531,6 @@ static bsq_status run_norm(bsq_format fmt, const void* x, const void* residual, 
     p.gate = (const T*)gate;
     p.rows = rows;
     p.C = (int)C;
-    p.inv_c = (float)(1.0 / (double)C);
     p.scale = scale;
     p.eps = eps;
     p.post_weight = post_weight;
@@ -594,7 +598,6 @@ static bsq_status run_norm_bwd(const void* gy, const void* gh, const void* h, co
     p.scale = scale;
     p.rows = rows;
     p.C = (int)C;
-    p.inv_c = (float)(1.0 / (double)C);
     p.grad_residual = (T*)grad_residual;
     p.grad_x = (T*)grad_x;
     p.grad_gate = (T*)grad_gate;
