@@ -445,16 +445,22 @@ static void launch_norm_have(int have, const NormArgs<T>& p, cudaStream_t st) {
 }
 
 // Four chunks to a thread spread a row's reductions (some 30 instructions per
-// warp each) over 32 elements, and 85 registers leave room for three CTAs of
-// 256 threads: 16384 x 7168 with post-norm and gate 185 us, with two chunks
-// and 512 threads 201 us, with three and 384 187 us.  One warp holds rows of
-// up to 256 elements a chunk per lane; longer rows take more threads.
+// warp each) over 32 elements (16384 x 7168 bf16 to MXFP8 with post-norm and
+// gate 188 us; with two chunks and 512 threads 16 us more, with three and 384
+// threads 2).  An SM's registers are to hold three CTAs of 256 threads; two for
+// fp32 rows, which take twice the registers in flight.  us with two, three and
+// four CTAs:
+//   16384 x 7168 bf16 to MXFP8, post-norm and gate 214, 188, 197, neither 163, 139, 137
+//   4096 x 7168 fp32 to MXFP8, post-norm and gate 89, 122, 127, neither 65, 68, 73
+// One warp holds rows of up to 256 elements a chunk per lane; longer rows take
+// more threads.
 template <typename T, int FMT>
 static void launch_norm(const NormArgs<T>& p, cudaStream_t st) {
     const int64_t n = p.C / 8;
     const int have = (p.post_weight ? kPost : 0) | (p.gate ? kGate : 0) | (p.residual ? kStream : 0);
+    constexpr int kCtas = sizeof(T) == 4 ? 2 : 3;
     if (n <= 32) launch_rows<norm_quant_kernel<T, FMT, 1, 32, 16, kAny, true>>(p.rows, 32, st, p);
-    else if (n <= 1024) launch_norm_have<T, FMT, 4, 256, 3>(have, p, st);
+    else if (n <= 1024) launch_norm_have<T, FMT, 4, 256, kCtas>(have, p, st);
     else if (n <= 2048) launch_norm_have<T, FMT, 2, 1024, 1>(have, p, st);
     else if (n <= 2560) launch_norm_have<T, FMT, 4, 640, 1>(have, p, st);
     else launch_rows<norm_quant_kernel<T, FMT, 4, 1024, 1, kAny, false>>(p.rows, row_threads(n, 4), st, p);
