@@ -93,8 +93,11 @@ struct Chunks {
 };
 
 // (sum / C + eps)^-1/2, each step rounded to nearest: a row's factor is in all
-// of its codes, so it is multiplied in by itself too, not folded into the
-// residual scale or the weights first.
+// of its codes.  It is multiplied in by itself too: folded into the residual
+// scale first, that product's rounding would be in all of them as well.  (The
+// weights differ by column, and weight * rstd first costs nothing in accuracy
+// and less time: 16384 x 7168 bf16 to NVFP4 with post-norm and gate 214 us,
+// after h * rstd 224.)
 __device__ __forceinline__ float rms_factor(float sum, int C, float eps) {
     return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)C), eps));
 }
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_quant_kernel(NormArgs<T> p) {
             const uint32_t at = ch.at(i);
             float w[8];
             load_weight(p.weight, at, w);
-            mul8(h[i], rstd);
+            mul8(w, rstd);
             mul8(h[i], w);
         }
         const float g = quantize_row<FMT, NCH>(h, p.C / 8, p.codes + base * kCodeBits / 8, p.scales + base / kBlock, red);
