@@ -132,9 +132,9 @@ __global__ void __launch_bounds__(kThreads, 8) swiglu_flat_kernel(const T* __res
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 6) swiglu_bwd_kernel(const T* __restrict__ gy, const T* __restrict__ x,
+__global__ void __launch_bounds__(kThreads, 6) swiglu_bwd_kernel(const T* __restrict__ gy, const T* x,
                                                                  FastDiv row_chunks, int64_t nchunks, int F,
-                                                                 T* __restrict__ gx) {
+                                                                 T* gx) {  // gx may be x
     const int64_t stride = (int64_t)gridDim.x * kThreads;
     for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < nchunks; c += stride) {
         const uint32_t row = fdiv((uint32_t)c, row_chunks);

@@ -90,3 +90,17 @@ def test_gates_past_every_border_stay_finite(B):
         assert bool(((row - want).abs() <= 16 * U * want + 2.0 ** -110).all())
         assert bool(((gx[:, 16] - want).abs() <= 2.0 ** -8 * want + 2.0 ** -110).all())
         assert bool(((gx[:, 0] - (want > 0).double()).abs() <= 2.0 ** -8).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,F", [(1, 8), (700, 2064), (3, 18432)])
+def test_activation_backward_in_place(B, dtype, rows, F):
+    """grad_x may be x itself: the same bits as into a tensor of its own."""
+    g = torch.Generator(device="cuda").manual_seed(F)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x = (2 * torch.randn(rows, 2 * F, generator=g, device="cuda")).to(dt)
+    gy = torch.randn(rows, F, generator=g, device="cuda").to(dt)
+    want = B.bsq_swiglu_backward(gy, x)
+    got = B.bsq_swiglu_backward(gy, x, grad_x=x)
+    torch.cuda.synchronize()
+    assert got is x and torch.equal(got, want)
