@@ -190,46 +190,34 @@ __device__ __forceinline__ float2 dot8(const float a[8], const float b[8], float
     return s;
 }
 
-// 8 elements that a thread copied to its own place in shared memory.
-template <typename T>
-__device__ __forceinline__ void raw_from_smem(Raw8<T>& r, const uint4* p, int stride);
-template <>
-__device__ __forceinline__ void raw_from_smem<uint16_t>(Raw8<uint16_t>& r, const uint4* p, int) {
-    r.r = p[0];
-}
-template <>
-__device__ __forceinline__ void raw_from_smem<float>(Raw8<float>& r, const uint4* p, int stride) {
-    const uint4 a = p[0], b = p[stride];
-    r.a = make_float4(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w));
-    r.b = make_float4(__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w));
-}
-
-// CTAs of KERNEL that one SM holds at `threads` threads, from the occupancy
-// calculator; cached per device and thread count.
-// and `smem` bytes of dynamic shared memory (which it may be given: 0 if not).
+// CTAs of KERNEL that one SM holds at `threads` threads and `smem` bytes of
+// dynamic shared memory (0 where it may not be given that many), from the
+// occupancy calculator; the latest kResidentKept answers are kept.
+constexpr int kResidentKept = 64;
 template <auto KERNEL>
 static inline int resident_rows(int threads, int smem = 0) {
     struct Entry {
-        int smem, n;
+        int dev, threads, smem, n;  // n + 1; 0: none yet
     };
-    static Entry cache[64][33] = {};
+    static Entry kept[kResidentKept] = {};
+    static int next = 0;
     static std::mutex mu;
+    int dev = -1;
+    cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lock(mu);
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-    Entry& e = cache[dev][threads / 32];
-    if (e.n == 0 || e.smem != smem) {  // the shared-memory opt-in stays as it is once made
-        int v = 0;
-        if ((smem > 0 && cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRowSmem) != cudaSuccess) ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, KERNEL, threads, smem) != cudaSuccess || v <= 0) {
-            cudaGetLastError();
-            v = smem > 0 ? 0 : 1;
-        }
-        e.smem = smem;
-        e.n = v;
-        return v;
+    for (const Entry& e : kept) {
+        if (e.n == 0) break;
+        if (e.dev == dev && e.threads == threads && e.smem == smem) return e.n - 1;
     }
-    return e.n;
+    int n = 0;
+    if ((smem > 0 && cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRowSmem) != cudaSuccess) ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, threads, smem) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = smem > 0 ? 0 : 1;
+    }
+    kept[next] = {dev, threads, smem, n + 1};
+    next = (next + 1) % kResidentKept;
+    return n;
 }
 
 // One wave of CTAs, a row each at a time.
