@@ -575,6 +575,13 @@ BSQ_API bsq_status bsq_norm_quantize(bsq_format fmt, const void* x, const void* 
     if (overlap(h, bytes, gate, bytes) || (h != x && overlap(h, bytes, x, bytes)) ||
         (h != residual && overlap(h, bytes, residual, bytes)))
         return fail(BSQ_ERR_INVALID_ARG, "%s: h overlaps an input (it may be x or residual itself)", fn);
+    const size_t n = (size_t)(rows * C), per_row = (size_t)rows * 4, per_col = (size_t)C * 4;
+    const Span outs[] = {{codes, fmt == BSQ_MXFP8 ? n : n / 2}, {scales, n / fmt_block(fmt)},
+                         {fmt == BSQ_NVFP4 ? row_scale : nullptr, per_row}, {rstd, per_row},
+                         {post_weight ? post_rstd : nullptr, per_row}};
+    const Span read[] = {{x, bytes}, {residual, bytes}, {gate, bytes}, {weight, per_col}, {post_weight, per_col}, {h, bytes}};
+    if (any_overlap(outs, read) || overlap(h, bytes, weight, per_col) || overlap(h, bytes, post_weight, per_col))
+        return fail(BSQ_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
     cudaStream_t st = (cudaStream_t)stream;
     return t == BSQ_BF16 ? run_norm<uint16_t>(fmt, x, residual, gate, rows, C, residual_scale, post_weight, weight, eps, h,
                                               codes, scales, row_scale, rstd, post_rstd, st, fn)
@@ -671,6 +678,13 @@ BSQ_API bsq_status bsq_norm_quantize_backward(const void* grad_y, const void* gr
     const size_t need = bsq_norm_backward_scratch_bytes(rows, C, post_weight != nullptr);
     if (scratch_bytes < need)
         return fail(BSQ_ERR_INVALID_ARG, "%s: scratch of %zu bytes, need %zu", fn, scratch_bytes, need);
+    const size_t per_row = (size_t)rows * 4, per_col = (size_t)C * 4;
+    const Span written[] = {{grad_residual, bytes}, {grad_x, bytes}, {grad_gate, bytes}, {grad_weight, per_col},
+                            {post_weight ? grad_post_weight : nullptr, per_col}, {scratch, need}};
+    const Span read[] = {{grad_y, bytes}, {grad_h, bytes}, {h, bytes}, {needs_x ? x : nullptr, bytes}, {gate, bytes},
+                         {weight, per_col}, {post_weight, per_col}, {rstd, per_row}, {post_weight ? post_rstd : nullptr, per_row}};
+    if (any_overlap(written, read))
+        return fail(BSQ_ERR_INVALID_ARG, "%s: an output or the scratch overlaps an input or another output", fn);
     const void* xin = needs_x ? x : nullptr;
     return t == BSQ_BF16
                ? run_norm_bwd<uint16_t>(grad_y, grad_h, h, rstd, weight, xin, gate, post_weight, post_rstd, residual_scale,

@@ -23,11 +23,6 @@ static inline bsq_status check_quant_format(const char* fn, bsq_format f) {
     return BSQ_OK;
 }
 
-// Do [a, a + na) and [b, b + nb) share a byte?
-static inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    return a && b && (const char*)a < (const char*)b + nb && (const char*)b < (const char*)a + na;
-}
-
 // Sums and maxima over the threads of a CTA, one barrier each: consecutive
 // reductions of a kernel alternate between two 32-float halves of `buf`, so a
 // thread that still reads one half is behind the barrier of the next before

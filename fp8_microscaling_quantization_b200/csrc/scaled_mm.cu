@@ -1105,12 +1105,21 @@ BSQ_API bsq_status bsq_grouped_mm_scaled(bsq_format a_fmt, bsq_format w_fmt, con
         ((uintptr_t)a_row_scale % 4) || ((uintptr_t)w_row_scale % 4) || ((uintptr_t)offs % 4) || ((uintptr_t)err % 4))
         return fail(BSQ_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
 
+    const int64_t row_bytes = (kind == MMA_MX8) ? K : K / 2;  // of an activation row
+    const int64_t row_scales = K / (kind == MMA_NVFP4 ? 16 : 32);
+    const int64_t w_row_bytes = wide_w ? K / 2 : row_bytes, w_rows = (int64_t)E * N;
+    const bool nv = kind == MMA_NVFP4;
+    const Span outs[] = {{out, (size_t)(T * N) * 2}, {err, 4}};
+    const Span read[] = {{a_codes, (size_t)(T * row_bytes)}, {a_scales, (size_t)(T * row_scales)},
+                         {nv ? a_row_scale : nullptr, (size_t)T * 4}, {w_codes, (size_t)(w_rows * w_row_bytes)},
+                         {w_scales, (size_t)(w_rows * row_scales)}, {nv ? w_row_scale : nullptr, (size_t)w_rows * 4},
+                         {offs, (size_t)E * 4}};
+    if (any_overlap(outs, read)) return fail(BSQ_ERR_INVALID_ARG, "%s: an output overlaps an input or the error word", fn);
+
     bsq_status st;
     smm::EncodeTiledFn encode = smm::encode_fn(&st, fn);
     if (!encode) return st;
     smm::Launch l;
-    const int64_t row_bytes = (kind == MMA_MX8) ? K : K / 2;  // of an activation row
-    const int64_t row_scales = K / (kind == MMA_NVFP4 ? 16 : 32);
     // The most tiles there can be; ragged experts end in partial ones.
     auto tiles = [&](int features, int tokens) {
         const int64_t f = (N + features - 1) / features;
@@ -1143,7 +1152,7 @@ BSQ_API bsq_status bsq_grouped_mm_scaled(bsq_format a_fmt, bsq_format w_fmt, con
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     };
     map(&l.x, a_codes, row_bytes, T, 0, smm::BKB, pairs ? tn / 2 : tn, false, true);
-    map(&l.w, w_codes, wide_w ? K / 2 : row_bytes, N, E, smm::BKB, smm::WM, wide_w, true);
+    map(&l.w, w_codes, w_row_bytes, N, E, smm::BKB, smm::WM, wide_w, true);
     if (raw) {
         const int chunk = smm::raw_row_bytes(kind);
         map(&l.sx, a_scales, row_scales, T, 0, chunk, tn, false, false);

@@ -196,6 +196,11 @@ BSQ_API bsq_status bsq_swiglu_quantize(bsq_format fmt, const void* x, bsq_dtype 
     if (!codes || !scales || (fmt == BSQ_NVFP4 && !row_scale)) return fail(BSQ_ERR_INVALID_ARG, "%s: null pointer", fn);
     if (!aligned(x, 16) || !aligned(codes, 8) || !aligned(row_scale, 4))
         return fail(BSQ_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    const size_t n = (size_t)(rows * F);
+    const Span outs[] = {{codes, fmt == BSQ_MXFP8 ? n : n / 2}, {scales, n / fmt_block(fmt)},
+                         {fmt == BSQ_NVFP4 ? row_scale : nullptr, (size_t)rows * 4}};
+    const Span read[] = {{x, 2 * n * (t == BSQ_BF16 ? 2 : 4)}};
+    if (any_overlap(outs, read)) return fail(BSQ_ERR_INVALID_ARG, "%s: an output overlaps x or another output", fn);
     cudaStream_t st = (cudaStream_t)stream;
     if (t == BSQ_BF16) launch_swiglu_fmt<uint16_t>(fmt, x, rows, F, codes, scales, row_scale, st);
     else launch_swiglu_fmt<float>(fmt, x, rows, F, codes, scales, row_scale, st);

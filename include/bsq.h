@@ -303,6 +303,7 @@ bsq_status bsq_grouped_mm_fp4(bsq_format fmt, bsq_dir dir, const void* a, const 
  * scale (0xFF, NVFP4 0x7F) makes the outputs it scales NaN and no others.
  * Its grad_x for frozen weights is bsq_grouped_mm_fp4 with BSQ_BWD, or this
  * product with grad_out and the transposed weights quantized along N.
+ * Neither out nor err may overlap an input or one another.
  * Requirements: K % 32 == 0 (K % 128 == 0 for MXFP8 x MXFP4), N % 8 == 0,
  * E <= 1024; a_codes, w_codes and out 16-byte aligned (w_codes 32-byte for
  * MXFP8 x MXFP4).  Other shapes return BSQ_ERR_UNSUPPORTED.  The waits are
@@ -331,6 +332,7 @@ bsq_status bsq_grouped_mm_scaled(bsq_format a_fmt, bsq_format w_fmt, const uint8
  *   codes, scales, row_scale  out, as bsq_quantize_<fmt> (row_scale: NVFP4)
  *   rstd, post_rstd    fp32 [rows] out: the two rsqrt factors (post_rstd
  *                      with post_weight only), kept for the backward pass
+ * No other output may overlap an input or another output (rejected).
  * C <= 32768, else BSQ_ERR_UNSUPPORTED. */
 bsq_status bsq_norm_quantize(bsq_format fmt, const void* x, const void* residual, const void* gate, bsq_dtype t,
                              int64_t rows, int64_t C, float residual_scale, const float* post_weight,
@@ -353,9 +355,10 @@ bsq_status bsq_norm_quantize(bsq_format fmt, const void* x, const void* residual
  * post_rstd are the forward's.  x is needed with a gate or post_weight only.
  * grad_residual or grad_x may be NULL (not stored; grad_x is needed with a
  * gate or post_weight).  Without gate, post_weight and residual_scale
- * grad_x equals grad_residual.  No output may overlap an input or another
- * output.  Weight gradients are fp32 [C], summed over the rows in an order
- * that depends on the shape and the device alone; with no rows they are 0.
+ * grad_x equals grad_residual.  Neither an output nor the scratch may overlap
+ * an input or another output (rejected).  Weight gradients are fp32 [C], summed
+ * over the rows in an order that depends on the shape and the device alone;
+ * with no rows they are 0.
  *   scratch  caller-owned device buffer of at least
  *            bsq_norm_backward_scratch_bytes(rows, C, post_weight != NULL)
  *            bytes, 16-byte aligned, no initialisation needed; calls that may
@@ -375,8 +378,9 @@ bsq_status bsq_norm_quantize_backward(const void* grad_y, const void* grad_h, co
  * (13 * 2**-24 of y off at most; 0 where g < -87.3, past the reciprocal's range),
  * quantized by the rules of bsq_quantize_<fmt> for a binary32 input, fmt
  * BSQ_NVFP4 (F % 16 == 0), BSQ_MXFP4 or BSQ_MXFP8 (F % 32 == 0), F <= 32768.
- * codes, scales and row_scale as there.  (The quantization pages take the
- * activations as given; no counterpart.) */
+ * codes, scales and row_scale as there; none may overlap x or another output
+ * (rejected).  (The quantization pages take the activations as given; no
+ * counterpart.) */
 bsq_status bsq_swiglu_quantize(bsq_format fmt, const void* x, bsq_dtype t, int64_t rows, int64_t F, uint8_t* codes,
                                uint8_t* scales, float* row_scale, bsq_stream_t stream);
 
