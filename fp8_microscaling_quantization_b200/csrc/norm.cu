@@ -23,15 +23,22 @@
 //   grad_x           = rx * (b - xhat * mean(b * xhat)), b = du * post_weight
 //                      (du without post_weight)
 //
-// One CTA holds a row in registers, so every tensor is read once and written
-// once: bound by HBM for many rows and by the barriers of the row's two or
-// three reductions for few.  Rows overlap because several CTAs share an SM
-// (registers are bounded for three); copying a thread's part of the next row
-// ahead with cp.async instead was slower, by its instructions (16384 x 7168
-// with post-norm and gate: 219 us against 185).  The weight gradients' sums
-// of a CTA's rows stay in shared memory, each thread adding to its own
-// columns; the CTAs' partial sums go to scratch and a second kernel adds them
-// in a fixed order.
+// One CTA holds a row: bound by HBM for many rows and by the barriers of the
+// row's two or three reductions for few.  Rows overlap because several CTAs
+// share an SM; copying a thread's part of the next row ahead with cp.async
+// instead was slower, by its instructions (16384 x 7168 bf16 to MXFP8 with
+// post-norm and gate: 219 us against 185 at the time).
+//   Forward: up to 20480 columns the row's inputs stay in registers and every
+// tensor is read once; longer rows read x a second time if there is a norm
+// after the block (from L2).  Which optional operands there are is known at
+// compile time from 257 to 20480 columns.
+//   Backward: up to 8192 columns (bf16: 16384) the inputs stay in registers;
+// longer rows read h, and with post_weight x, a second time.  The sums of the
+// weight gradients over a CTA's rows, each thread's own columns, are in
+// registers up to 8192 columns, then in shared memory, or, where that does not
+// hold them, in the CTA's row of the scratch; a second kernel adds the CTAs'
+// sums in a fixed order.  Optional operands are known at compile time from 257
+// to 8192 columns.
 #include <algorithm>
 
 #define BSQ_DBG_FILE 8
@@ -421,7 +428,7 @@ __global__ void __launch_bounds__(256) norm_weight_sum_kernel(const float* __res
     if (c < C) {
 #pragma unroll 8
         for (int r = slice; r < n; r += 32) {
-            // from L2: the sums are written while this kernel may be resident
+            // each read once: from L2, past L1
             const float4 t = __ldcg(reinterpret_cast<const float4*>(p + (int64_t)r * C + c));
             v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
         }
@@ -621,7 +628,8 @@ static bsq_status run_norm_bwd(const void* gy, const void* gh, const void* h, co
     p.partial_post = scratch + (size_t)max_ctas * C;
     const int ctas = launch_norm_bwd<T>(p, max_ctas, st);
     BSQ_TRY(check_launch(fn));
-    // launched while the CTAs above still run; it waits for them itself
+    // a programmatic launch: it may start when the last CTA above has ended, and
+    // waits itself until what that wrote is visible
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
