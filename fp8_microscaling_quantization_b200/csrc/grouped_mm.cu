@@ -59,6 +59,7 @@
 #include "formats.cuh"
 #include "host_util.h"
 #include "pipeline_drain.h"
+#include "tma_encode.h"
 #include "tcgen05.cuh"
 
 namespace bsq {
@@ -760,29 +761,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_mm_kernel(const __grid_co
 
 // ----------------------------------------------------------------- host -----
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn(bsq_status* st) {
-    static std::mutex mu;
-    static EncodeTiledFn fn = nullptr;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
-        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !p) {
-            *st = fail(BSQ_ERR_CUDA, "bsq_grouped_mm_fp4: cuTensorMapEncodeTiled unavailable (%s)",
-                       cudaGetErrorString(e));
-            return nullptr;
-        }
-        fn = (EncodeTiledFn)p;
-    }
-    *st = BSQ_OK;
-    return fn;
-}
-
 template <int FMT, int DIR, int CG>
 static bsq_status launch_gmm(const CUtensorMap& tmap, const gmm::Args& a, int64_t max_groups, cudaStream_t st) {
     static std::mutex mu;
@@ -856,7 +834,7 @@ BSQ_API bsq_status bsq_grouped_mm_fp4(bsq_format fmt, bsq_dir dir, const void* a
         return fail(BSQ_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
 
     bsq_status st;
-    EncodeTiledFn encode = encode_fn(&st);
+    EncodeTiledFn encode = encode_fn(&st, fn);
     if (!encode) return st;
     CUtensorMap tmap;
     const cuuint64_t dims[2] = {(cuuint64_t)contr, (cuuint64_t)T};

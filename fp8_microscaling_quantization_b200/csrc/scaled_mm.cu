@@ -75,6 +75,7 @@
 #include "common.cuh"
 #include "host_util.h"
 #include "pipeline_drain.h"
+#include "tma_encode.h"
 #include "scaled_tc.cuh"
 
 namespace bsq {
@@ -969,28 +970,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ----------------------------------------------------------------- host -----
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn(bsq_status* st, const char* fn_name) {
-    static std::mutex mu;
-    static EncodeTiledFn fn = nullptr;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
-        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !p) {
-            *st = fail(BSQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable (%s)", fn_name, cudaGetErrorString(e));
-            return nullptr;
-        }
-        fn = (EncodeTiledFn)p;
-    }
-    *st = BSQ_OK;
-    return fn;
-}
-
 struct Launch {
     CUtensorMap x, w, sx, sw, out;
     Args args;
@@ -1117,7 +1096,7 @@ BSQ_API bsq_status bsq_grouped_mm_scaled(bsq_format a_fmt, bsq_format w_fmt, con
     if (any_overlap(outs, read)) return fail(BSQ_ERR_INVALID_ARG, "%s: an output overlaps an input or the error word", fn);
 
     bsq_status st;
-    smm::EncodeTiledFn encode = smm::encode_fn(&st, fn);
+    EncodeTiledFn encode = encode_fn(&st, fn);
     if (!encode) return st;
     smm::Launch l;
     // The most tiles there can be; ragged experts end in partial ones.
