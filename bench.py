@@ -95,7 +95,7 @@ KERNEL_SOURCES = {
     "cache": ["cache.cu", "common.cuh", "formats.cuh", "host_util.h", "debug.cuh"],
     "static": ["static.cu", "common.cuh", "formats.cuh", "host_util.h", "debug.cuh"],
     "kv": ["kv_cache.cu", "common.cuh", "formats.cuh", "host_util.h", "debug.cuh"],
-    "gemm": ["grouped_mm.cu", "tcgen05.cuh", "formats.cuh", "host_util.h", "debug.cuh"],
+    "gemm": ["grouped_mm.cu", "tcgen05.cuh", "pipeline_drain.h", "tma_encode.h", "formats.cuh", "host_util.h", "debug.cuh"],
 }
 
 

@@ -24,7 +24,7 @@ LIB_DEBUG = os.path.join(HERE, "libbsq_debug.so")
 SOURCES = ["abi.cu", "flat.cu", "nvfp4.cu", "static.cu", "kv_cache.cu", "cache.cu", "grouped_mm.cu",
            "scaled_mm.cu", "norm.cu", "swiglu.cu"]
 HEADERS = ["common.cuh", "formats.cuh", "host_util.h", "tcgen05.cuh", "debug.cuh", "scaled_tc.cuh", "row_quant.cuh",
-           "pipeline_drain.h", "tma_encode.h"]
+           "pipeline_drain.h", "tma_encode.h", "overlap.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -59,8 +59,8 @@
 #include "formats.cuh"
 #include "host_util.h"
 #include "pipeline_drain.h"
-#include "tma_encode.h"
 #include "tcgen05.cuh"
+#include "tma_encode.h"
 
 namespace bsq {
 using namespace sm100;

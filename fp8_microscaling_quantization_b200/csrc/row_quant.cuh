@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "overlap.h"
 
 namespace bsq {
 

@@ -74,9 +74,10 @@
 #include "debug.cuh"
 #include "common.cuh"
 #include "host_util.h"
+#include "overlap.h"
 #include "pipeline_drain.h"
-#include "tma_encode.h"
 #include "scaled_tc.cuh"
+#include "tma_encode.h"
 
 namespace bsq {
 using namespace sm100;
