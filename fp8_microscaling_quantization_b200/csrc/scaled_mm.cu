@@ -24,8 +24,8 @@
 // them: blocks of 128 rows x 4 bytes, the bytes of row r at (r % 32) * 16 +
 // (r / 32) * 4.  Scale rows that TMA cannot read, of other than a multiple of
 // 16 bytes, are loaded by the four warps themselves, which costs the memory
-// pipe a request per row (4096 x 4096 x 2080 against 2048: NVFP4 62 us
-// against 23, MXFP8 48 against 35).  The MMA warp copies the blocks to a ring
+// pipe a request per row (4096 x 4096 x 2080 against 2048: NVFP4 63 us
+// against 27, MXFP8 48 against 35).  The MMA warp copies the blocks to a ring
 // of tensor-memory slots and issues the k-step's MMAs.
 //
 // Persistent, warp-specialised CTA of 480 threads (one per SM):
