@@ -1,4 +1,4 @@
-// tma_encode.h -- the driver's tensor-map encoder, found once per process.
+// tma_encode.h -- the CUDA driver's tensor-map encoder, found once per process.
 #pragma once
 
 #include <cuda.h>
@@ -14,7 +14,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// NULL, with the reason in *st, where the driver has none.
+// NULL, with the reason in *st, where the CUDA driver has none.
 static inline EncodeTiledFn encode_fn(bsq_status* st, const char* caller) {
     static std::mutex mu;
     static EncodeTiledFn fn = nullptr;
